@@ -14,6 +14,7 @@
 #include <mutex>
 #include <string>
 #include <unordered_map>
+#include <unordered_set>
 #include <utility>
 #include <vector>
 
@@ -74,7 +75,7 @@ struct zs_ctx {
   int64_t coop_max_grid = INT64_MAX;  // lowered when the runtime refuses a cooperative grid
   std::string err;
   std::unordered_map<const void*, int> occupancy;  // resident CTAs per SM, per kernel
-  std::unordered_map<const void*, int> smem_allowed;  // dynamic shared memory, per kernel
+  std::unordered_set<const void*> smem_allowed;  // kernels whose dynamic shared memory is raised
   int64_t launches = 0;
   bool pdl = true;  // launch the step's kernels as programmatic dependents
   bool coop_pdl = true;  // the fused step's cooperative launch too (off once refused)
