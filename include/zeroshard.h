@@ -625,7 +625,8 @@ zs_status zs_engine_state(const zs_engine* e, int64_t* global_steps, int64_t* ap
  * holds the first moment so; v holds the ROOT of the second, sqrt(v), and an
  * element whose root is above zero keeps at least the least code (2^-9): the
  * root's value is code * c.  The update uses the moments of this step before
- * they are rounded.  Moments start at zero bytes and zero scales.  The averaged
+ * they are rounded.  A block holding an inf or NaN has a scale that is not finite
+ * and reads back as inf or NaN.  Moments start at zero bytes and zero scales.  The averaged
  * gradient is held to +-2^63 in this form, where its square would leave fp32. */
 #define ZS_STATE_BLOCK 256
 typedef enum { ZS_STATES_FP32 = 0, ZS_STATES_8BIT = 1 } zs_states;

@@ -24,7 +24,8 @@
 // root halves v's range in binades, so that E4M3's 17 binades hold |g| ratios
 // of 2^17 within a block, and r > 0 never rounds to 0 (it keeps at least the
 // least code, 2^-9): a lost second moment would divide a living first moment
-// by eps.  The scale is fp32 and not a power of two so that a block whose
+// by eps.  An inf or NaN among a block's values makes its scale inf or NaN, and the
+// block reads back so.  The scale is fp32 and not a power of two so that a block whose
 // values all decay by 0.1 % a step decays with it; a coarse scale would hold
 // it still.
 #pragma once
@@ -489,6 +490,20 @@ __device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
   return c < 0x1p-126f ? 0x1p-126f : c;
 }
 
+// The scale of a block of moments, as above with the quotient rounded once: the
+// state goes from step to step through it.
+__device__ __forceinline__ float state_scale(uint32_t amax_bits) {
+  const float c = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
+  return c < 0x1p-126f ? 0x1p-126f : c;
+}
+
+// x held to +-limit; a NaN stays one.
+__device__ __forceinline__ float held_to(float x, float limit) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-limit));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(limit));
+  return x;
+}
+
 // 1 / c and sqrt(v) to one unit in the last place or so: what follows them is
 // rounded to 4 bits, and the exact forms take ten instructions each.
 __device__ __forceinline__ float rcp_approx(float c) {
@@ -509,7 +524,7 @@ __device__ __forceinline__ float sqrt_approx(float v) {
 // gradient is held to +-2^63, where its square would leave fp32.
 __device__ __forceinline__ void adamw1_q8(const AdamArgs& ad, float g_mul, float sum, float& p,
                                           float& m, float& r) {
-  const float g = fminf(fmaxf(__fmul_rn(sum, g_mul), -0x1p63f), 0x1p63f);
+  const float g = held_to(__fmul_rn(sum, g_mul), 0x1p63f);
   m = __fmaf_rn(ad.beta1, m, __fmul_rn(ad.omb1, g));
   const float v = __fmaf_rn(__fmul_rn(ad.beta2, r), r, __fmul_rn(__fmul_rn(ad.omb2, g), g));
   r = sqrt_approx(v);
@@ -536,17 +551,17 @@ __device__ __forceinline__ void list_update(ListVals& x, const AdamArgs& ad, flo
       x.v[k] = __fmul_rn(x.v[k], vc);
       adamw1_q8(ad, g_mul, x.g[k], x.p[k], x.m[k], x.v[k]);
       mtop = max(mtop, __float_as_uint(x.m[k]) & 0x7fffffffu);
-      vtop = max(vtop, __float_as_uint(x.v[k]));
+      vtop = max(vtop, __float_as_uint(x.v[k]) & 0x7fffffffu);
     }
-    // the scales divided exactly: the state goes from step to step through them
-    // (with exact reciprocals too a step is 1 % slower)
-    mc = fmaxf(__fdiv_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, mtop)), 448.0f), 0x1p-126f);
-    vc = fmaxf(__fdiv_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, vtop)), 448.0f), 0x1p-126f);
+    // (an inf or NaN has the largest bits: its block's scale is not finite)
+    mc = state_scale(__reduce_max_sync(0xffffffffu, mtop));
+    vc = state_scale(__reduce_max_sync(0xffffffffu, vtop));
     const float mi = rcp_approx(mc), vi = rcp_approx(vc);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       x.m[k] = __fmul_rn(x.m[k], mi);
-      x.v[k] = x.v[k] > 0.0f ? fmaxf(__fmul_rn(x.v[k], vi), 0x1p-9f) : 0.0f;
+      const float q = __fmul_rn(x.v[k], vi);
+      x.v[k] = x.v[k] > 0.0f && q < 0x1p-9f ? 0x1p-9f : q;
     }
   } else {
 #pragma unroll
