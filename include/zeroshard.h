@@ -608,7 +608,8 @@ zs_status zs_engine_state(const zs_engine* e, int64_t* global_steps, int64_t* ap
  * parameters that are not one flat shard: norm weights, biases, embeddings, a
  * model whose tensors live where its framework put them.  Two launches
  * whatever the number of tensors; the result of a tensor with 32-bit moments
- * is bit for bit that of zs_apply on it.
+ * is bit for bit that of zs_apply on it, or of zs_apply_clipped with the same
+ * sum of squares.
  *
  * A step reads every gradient, decides the overflow and the global norm over
  * all of them before any state is written, then updates every tensor:

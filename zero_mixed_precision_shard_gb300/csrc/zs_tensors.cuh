@@ -289,14 +289,9 @@ struct ListCursor {
 };
 
 // Norm and clipping coefficient of the averaged gradient's sum of squares, in
-// fp32 (a chain of fp64 roots and divisions by one thread takes over a
-// microsecond here); fp64 where the sum leaves fp32.
+// fp64 and rounded once, as the flat step forms them: what one norm over
+// several lists and shards clips is scaled alike everywhere.
 __device__ __forceinline__ float list_coef(double sumsq, float max_norm, float* norm) {
-  if (sumsq == 0.0 || (sumsq > 1e-30 && sumsq < 1e38)) {
-    *norm = __fsqrt_rn((float)sumsq);
-    if (!(max_norm > 0.0f)) return 1.0f;
-    return fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(*norm, 1e-6f)));
-  }
   const double n = sqrt(sumsq);
   *norm = (float)n;
   return clip_coef_of_norm(n, max_norm);
