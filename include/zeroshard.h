@@ -691,7 +691,8 @@ zs_status zs_tensors_step_async(zs_tensors* t, int32_t n, int32_t accum_steps,
  * lists, shards or GPUs.  Phase 1 ORs into the device int32 *d_flag whether
  * any gradient is inf or NaN, and writes *d_sumsq (device fp64, may be NULL) =
  * the sum of (g / grad_div)^2, a thread's squares added in fp32 with the
- * rounding carried along, the CTAs' sums in fp64, in an order fixed by the list
+ * rounding carried along (values whose squares would leave fp32 at either end
+ * apart, scaled), the CTAs' sums in fp64, in an order fixed by the list
  * and the device (deterministic).  Phase 2 updates unless
  * *d_flag != 0; d_sumsq NULL or max_norm <= 0: no clipping; step is Adam's
  * 1-based count.  Neither clears *d_flag. */

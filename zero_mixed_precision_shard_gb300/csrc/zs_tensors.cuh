@@ -109,18 +109,25 @@ struct ListFinish {
   double inv_div2;
 };
 
-// The square of one gradient value where a thread's sum says that some value
-// may be large: past 1e15 in magnitude it is scaled by 2^-80 first and summed
-// apart, so that neither sum leaves fp32.  An inf or NaN makes its sum inf or
-// NaN and stays visible to the end.
-__device__ __forceinline__ void list_sq(float g, float& sqf, float& sqb) {
-  if (fabsf(g) > 1e15f) {
-    const float t = __fmul_rn(g, 0x1p-80f);
-    sqb = __fmaf_rn(t, t, sqb);
-  } else {
-    sqf = __fmaf_rn(g, g, sqf);
+// Squares of single gradient values, summed apart by size so that none leaves
+// fp32 at either end: past 1e15 in magnitude a value is scaled by 2^-80 first,
+// below 2^-55 by 2^100 (its least square is then 2^-98).  An inf or NaN makes its
+// sum inf or NaN and stays visible to the end.
+constexpr float kListLow = 0x1p-55f;
+struct ListSquares {
+  float mid = 0.0f, big = 0.0f, low = 0.0f;
+  __device__ __forceinline__ void add(float g) {
+    if (fabsf(g) > 1e15f) {
+      const float t = __fmul_rn(g, 0x1p-80f);
+      big = __fmaf_rn(t, t, big);
+    } else if (fabsf(g) < kListLow) {
+      const float t = __fmul_rn(g, 0x1p100f);
+      low = __fmaf_rn(t, t, low);
+    } else {
+      mid = __fmaf_rn(g, g, mid);
+    }
   }
-}
+};
 
 template <int DT>
 __device__ __forceinline__ void unpack8(const uint4 h, float a[8]) {
@@ -153,23 +160,40 @@ __device__ __forceinline__ void unpack16(const uint4 q, float (&a)[GT == ZS_FP32
 
 // A thread's sum of squares: what rounding cuts off each addition is carried
 // into the next, so that the sum of a thread that strides over a long list
-// keeps 32 bits.  `big` is the sum of the scaled squares.
+// keeps 32 bits.  `big` and `low` are the sums of the scaled squares.
 struct ListSum {
-  float sum = 0.0f, cut = 0.0f, big = 0.0f;
+  float sum = 0.0f, cut = 0.0f, big = 0.0f, low = 0.0f;
   __device__ __forceinline__ void add(float x) {
     const float y = __fsub_rn(x, cut);
     const float t = __fadd_rn(sum, y);
     cut = __fsub_rn(__fsub_rn(t, sum), y);
     sum = t;
   }
+  __device__ __forceinline__ void add(const ListSquares& q) {
+    add(q.mid);
+    big = __fadd_rn(big, q.big);
+    low = __fadd_rn(low, q.low);
+  }
 };
 
 // Gradients on their way through registers: kListBatch loads of 16 bytes.
 constexpr int kListBatch = 4;
 
+// Whether any of a batch's values is not a zero.
+template <int GT>
+__device__ __forceinline__ bool list_any(const uint4 (&q)[kListBatch]) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int j = 0; j < kListBatch; ++j) any |= q[j].x | q[j].y | q[j].z | q[j].w;
+  return (any & (GT == ZS_FP32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) != 0;
+}
+
 // Squares of a batch without a test (two instructions an element: the pass
 // would be bound by issue otherwise), and again, with one, where the sum is
-// large or not a number.
+// large, not a number, or so small that squares were lost in it: at 2^-110 the
+// 32 values' squares are off by at most 32 half units of 2^-149, 2^-35 of the
+// sum.  (A half has no square below 2^-48; batches of zeros are common, and left
+// at once.)
 template <int GT>
 __device__ __forceinline__ void list_squares(const uint4 (&q)[kListBatch], ListSum& s) {
   constexpr int kPer = GT == ZS_FP32 ? 4 : 8;
@@ -182,17 +206,18 @@ __device__ __forceinline__ void list_squares(const uint4 (&q)[kListBatch], ListS
     for (int k = 0; k < kPer; ++k) t[k & 1] = __fmaf_rn(a[k], a[k], t[k & 1]);
   }
   t[0] = __fadd_rn(t[0], t[1]);
-  if (t[0] < 1e30f) {
+  if (t[0] < 1e30f && (GT == ZS_FP16 || t[0] >= kListLow * kListLow)) {
     s.add(t[0]);
     return;
   }
-  float sq = 0.0f;
+  if (GT != ZS_FP16 && t[0] < 1e30f && !list_any<GT>(q)) return;
+  ListSquares sq;
 #pragma unroll
   for (int j = 0; j < kListBatch; ++j) {
     float a[kPer];
     unpack16<GT>(q[j], a);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) list_sq(a[k], sq, s.big);
+    for (int k = 0; k < kPer; ++k) sq.add(a[k]);
   }
   s.add(sq);
 }
@@ -205,9 +230,9 @@ __device__ __forceinline__ void list_ends(const E* g, int head, int64_t tail, in
   int64_t i = threadIdx.x;
   if (i >= head) i += tail - head;
   if (i >= n) return;
-  float sq = 0.0f;
-  if constexpr (GT == ZS_FP32) list_sq(g[i], sq, s.big);
-  else list_sq(half_bits_to_float<GT>(g[i]), sq, s.big);
+  ListSquares sq;
+  if constexpr (GT == ZS_FP32) sq.add(g[i]);
+  else sq.add(half_bits_to_float<GT>(g[i]));
   s.add(sq);
 }
 
@@ -409,7 +434,9 @@ __global__ void __launch_bounds__(kThreads, kListCheckCtas)
     fill(slot);
   }
   bool unused = false;
-  const double total = cta_norm_total(__fsub_rn(s.sum, s.cut), s.big, false, &unused);
+  double total = cta_norm_total(__fsub_rn(s.sum, s.cut), s.big, false, &unused);
+  if (__syncthreads_or(s.low != 0.0f))
+    total += cta_norm_total(s.low, 0.0f, false, &unused) * 0x1p-200;
   // the last CTA to finish folds the sums, in a fixed order whichever it is
   __shared__ int last;
   if (threadIdx.x == 0) {
