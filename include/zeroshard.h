@@ -622,13 +622,16 @@ zs_status zs_engine_state(const zs_engine* e, int64_t* global_steps, int64_t* ap
  * ZS_STATES_8BIT keeps the moments in one byte an element.  Every
  * ZS_STATE_BLOCK consecutive elements of a tensor (the last block may be
  * shorter) share an fp32 scale c = max|x| / 448, at least 2^-126, and an
- * element's byte is the OCP E4M3 value nearest to x / c (ties to even).  m
- * holds the first moment so; v holds the ROOT of the second, sqrt(v), and an
- * element whose root is above zero keeps at least the least code (2^-9): the
- * root's value is code * c.  The update uses the moments of this step before
- * they are rounded.  A block holding an inf or NaN has a scale that is not finite
- * and reads back as inf or NaN.  Moments start at zero bytes and zero scales.  The averaged
- * gradient is held to +-2^63 in this form, where its square would leave fp32. */
+ * element's byte is the OCP E4M3 value nearest to the fp32 quotient x / c (ties
+ * to even).  m holds the first moment so; v holds the ROOT of the second,
+ * sqrt(v), and an element whose root is above zero keeps at least the least code
+ * (2^-9): the root's value is code * c.  The update uses the moments of this step
+ * before they are rounded, which are bit for bit those of the 32-bit form from
+ * the decoded ones (but where the averaged gradient is subnormal); its own
+ * arithmetic is as good as that form's, in another order.  A block holding an inf
+ * or NaN has a scale that is not finite and reads back as inf or NaN.  Moments
+ * start at zero bytes and zero scales.  The averaged gradient is held to +-2^63
+ * in this form, where its square would leave fp32. */
 #define ZS_STATE_BLOCK 256
 typedef enum { ZS_STATES_FP32 = 0, ZS_STATES_8BIT = 1 } zs_states;
 

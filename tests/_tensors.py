@@ -89,8 +89,13 @@ def equal_bits(a, b):
 
 
 def assert_8bit_equals_32bit(zs, ctx, made, div, max_norm, t=3):
-    """One step of the 8-bit list against one of the 32-bit list from its decoded moments."""
-    wide = made.clone(states=0)
+    """One step of the 8-bit list against one of the 32-bit list from its decoded
+    moments: the new moments' bytes and scales bit for bit, and the weights within
+    the rounding of the update by 32-bit operations, in half units of 2^-24: of
+    the update 1 each for m_hat, the root, its bias correction, eps, the quotient and
+    the decay's addition (and 2^-4 for what a corrected quotient or root leaves), of
+    the decay 1, of the weight 1."""
+    wide, start = made.clone(states=0), [e["p"].double() for e in made.t]
     hp = zs.make_hparams(*HP)
     for x in (made, wide):
         lst = x.list(ctx)
@@ -98,8 +103,14 @@ def assert_8bit_equals_32bit(zs, ctx, made, div, max_norm, t=3):
         zs.zs_tensors_step_async(lst, 1, 1, hp, None, max_norm, d)
         assert d.read().overflow == 0
         lst.close()
-    for e, w in zip(made.t, wide.t):
-        assert torch.equal(e["p"], w["p"]) and torch.equal(e["h"], w["h"])
+    lr, b1, b2, eps, wd = (float(np.float32(x)) for x in HP)
+    for e, w, p0 in zip(made.t, wide.t, start):
+        m, v = w["m"].double() / (1 - b1 ** t), w["v"].double() / (1 - b2 ** t)
+        u = m / (v.sqrt() + eps)
+        want = p0 - lr * (u + wd * p0)
+        bound = 2.0 ** -24 * (lr * (6.0625 * u.abs() + wd * p0.abs()) + want.abs()) + 2.0 ** -149
+        assert ((e["p"].double() - want).abs() <= bound).all()
+        assert torch.equal(e["h"], e["p"].to(e["h"].dtype))
         for key, scale, x in (("m", "mc", w["m"]), ("v", "vc", torch.from_numpy(
                 np.sqrt(w["v"].cpu().numpy())))):
             codes, c = encode(x, key == "v")

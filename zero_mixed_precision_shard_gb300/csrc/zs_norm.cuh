@@ -115,13 +115,6 @@ struct RowShare {
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// max(|a|, |b|), NaN if either is.
-__device__ __forceinline__ float abs_max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
-  return r;
-}
-
 // The scale past which a row's sum of squares leaves fp32 (bf16 values from
 // about 1e18): squares of the values times 2^-100 instead (below 2^56, so that
 // 2^31 of them stay in fp32; eps is nothing beside them).  An inf or NaN in the

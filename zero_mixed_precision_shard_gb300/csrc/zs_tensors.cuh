@@ -10,7 +10,7 @@
 //
 // Both are bound by HBM (measured at 124M elements: the update moves 28 bytes
 // an element with fp16 gradients and 32-bit moments at 6.9 TB/s, 504 us, and 16
-// with 8-bit ones at 6.7 TB/s, 297 us; the check reads 2 at 5.9 TB/s).
+// with 8-bit ones at 6.4 TB/s, 310 us; the check reads 2 at 5.9 TB/s).
 //
 // The update's CTA takes one chunk of one tensor (the plan's chunk table, built
 // at creation), a warp a block of 256 elements at a time: through a ring of
@@ -64,15 +64,48 @@ struct ListChunk {
   int32_t index;   // chunk number within the tensor
 };
 
+// Constants of the update with 8-bit moments, which takes the bias corrections
+// and adamw1's eps together, root as an fp32 pair:
+//   (m * inv_bc1) / (r * sbc2 + eps) = m / (r * root + eps / inv_bc1)
+struct ListRatios {
+  float root, root_lo, eps;
+};
+
+// From 1 - beta1^t and sqrt(1 / (1 - beta2^t)).
+__host__ __device__ inline ListRatios list_ratios(double bc1, double sbc2, float eps) {
+  ListRatios r;
+  const double root = sbc2 * bc1;
+  r.root = (float)root;
+  r.root_lo = (float)(root - (double)r.root);
+  r.eps = (float)((double)eps * bc1);
+  return r;
+}
+
 // What the check pass leaves for the update.
 struct ListStep {
   AdamArgs ad;
   float coef;      // clipping coefficient, 1 without clipping
-  float g_mul;     // coef / grad_div
   int32_t skip;    // the step overflowed: write nothing
-  float inv_div;   // 1 / grad_div
+  float inv_div;   // exact_inverse(grad_div)
+  float g_mul;     // coef * inv_div, 0 where that is not exact
+  ListRatios ratios;
   double inv_div2; // 1 / grad_div^2
 };
+
+// 1 / d where that is exact (a power of two, as loss scales are), 0 where not:
+// a product with it is then the quotient by d, bit for bit.
+__device__ __forceinline__ float exact_inverse(float d) {
+  const uint32_t b = __float_as_uint(d), e = b >> 23;
+  return (b & 0x7FFFFFu) == 0u && e >= 1u && e <= 253u ? __uint_as_float((254u - e) << 23) : 0.0f;
+}
+
+// A product of the sum of gradients with coef * inv_div is the averaged and
+// clipped gradient as adamw1 forms it, by a quotient and a product, wherever the
+// averaged gradient is no subnormal.
+__device__ __forceinline__ float list_g_mul(float coef, float inv_div) {
+  const float x = __fmul_rn(coef, inv_div);
+  return x >= 0x1p-126f ? x : 0.0f;
+}
 
 // As pdl_enter, without letting the successor in early: it is launched when
 // this grid's last CTA exits.  The list's kernels fill the GPU to their end,
@@ -332,8 +365,7 @@ __device__ __forceinline__ void list_step_args(const ListFinish& fin, ListStep* 
   const float div = (float)((double)fin.n * (double)fin.accum_steps * (double)st->scaler.scale);
   if (lane == 2) step->ad.lr = fin.has_sched ? lr_at(fin.sched, t) : fin.hp.lr;
   if (lane == 3) {
-    const double inv = 1.0 / (double)div;
-    step->inv_div = (float)inv;
+    step->inv_div = exact_inverse(div);
     step->inv_div2 = 1.0 / ((double)div * (double)div);
     step->ad.grad_div = div;
     step->ad.beta1 = fin.hp.beta1;
@@ -343,21 +375,26 @@ __device__ __forceinline__ void list_step_args(const ListFinish& fin, ListStep* 
     step->ad.eps = fin.hp.eps;
     step->ad.wd = fin.hp.weight_decay;
   }
+  double mine = 0.0;  // lane 0: 1 - beta1^t, lane 1: sqrt(1 / (1 - beta2^t))
   if (lane < 2) {
-    const double inv = 1.0 / (1.0 - pow_int((double)(lane == 0 ? fin.hp.beta1 : fin.hp.beta2), t));
+    const double bc = 1.0 - pow_int((double)(lane == 0 ? fin.hp.beta1 : fin.hp.beta2), t);
+    const double inv = 1.0 / bc;
     const float hi = (float)inv;
     const float lo = (float)(inv - (double)hi);
     if (lane == 0) {
+      mine = bc;
       step->ad.inv_bc1 = hi;
       step->ad.inv_bc1_lo = lo;
     } else {
+      mine = sqrt(inv);
       step->ad.inv_bc2 = hi;
       step->ad.inv_bc2_lo = lo;
-      const double root = sqrt(inv);
-      step->ad.sbc2 = (float)root;
-      step->ad.sbc2_lo = (float)(root - (double)step->ad.sbc2);
+      step->ad.sbc2 = (float)mine;
+      step->ad.sbc2_lo = (float)(mine - (double)step->ad.sbc2);
     }
   }
+  const double sbc2 = __shfl_sync(0xffffffffu, mine, 1);
+  if (lane == 0) step->ratios = list_ratios(mine, sbc2, fin.hp.eps);
 }
 
 // The end of the check pass (one thread): the step resolved from the sum of
@@ -369,7 +406,7 @@ __device__ __forceinline__ void list_finish(const ListPlan& pl, const ListFinish
     float norm;
     const float coef = list_coef(sum * __ldcg(&pl.step->inv_div2), fin.max_norm, &norm);
     pl.step->coef = coef;
-    pl.step->g_mul = __fmul_rn(coef, __ldcg(&pl.step->inv_div));
+    pl.step->g_mul = list_g_mul(coef, __ldcg(&pl.step->inv_div));
     pl.step->skip = bad;
     AdamArgs ad;  // what device_state_step records
     ad.lr = __ldcg(&pl.step->ad.lr);
@@ -455,14 +492,16 @@ __global__ void __launch_bounds__(kThreads, kListCheckCtas)
 
 // The update's constants where the caller resolved the step (one thread).
 __global__ void k_list_args(const int32_t* __restrict__ flag, const double* __restrict__ sumsq,
-                            float max_norm, AdamArgs ad, ListStep* __restrict__ step) {
+                            float max_norm, AdamArgs ad, ListRatios ratios,
+                            ListStep* __restrict__ step) {
   pdl_enter(flag, sumsq, step);
   if (blockIdx.x != 0 || threadIdx.x != 0) return;
   float norm;
   const float coef = sumsq != nullptr ? list_coef(*sumsq, max_norm, &norm) : 1.0f;
   step->ad = ad;
   step->coef = coef;
-  step->g_mul = __fmul_rn(coef, (float)(1.0 / (double)ad.grad_div));
+  step->g_mul = list_g_mul(coef, exact_inverse(ad.grad_div));
+  step->ratios = ratios;
   step->skip = *flag != 0;
 }
 
@@ -526,32 +565,36 @@ __device__ __forceinline__ float held_to(float x, float limit) {
   return x;
 }
 
-// 1 / c and sqrt(v) to one unit in the last place or so: what follows them is
-// rounded to 4 bits, and the exact forms take ten instructions each.
 __device__ __forceinline__ float rcp_approx(float c) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(c));
   return r;
 }
 
-__device__ __forceinline__ float sqrt_approx(float v) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
+// x / c from the approximate reciprocal of c: a quotient 2 units off at most,
+// corrected by its own residual, which one fma forms (Markstein 1990).  What is
+// left beside the last rounding is 2^-21 of a unit.  For c in [2^-93, 2^126);
+// beside smaller ones the residual of small quotients leaves fp32.
+__device__ __forceinline__ float quotient(float x, float c, float rcp) {
+  const float q = __fmul_rn(x, rcp);
+  return __fmaf_rn(__fmaf_rn(-q, c, x), rcp, q);
 }
 
-// AdamW for 8-bit moments, r = sqrt(v): the arithmetic of adamw1 with
-// approximate division (2 ulp; the moments are about to be rounded to 4
-// bits, and lr * update is far below an ulp of most weights).  The averaged
-// gradient is held to +-2^63, where its square would leave fp32.
-__device__ __forceinline__ void adamw1_q8(const AdamArgs& ad, float g_mul, float sum, float& p,
-                                          float& m, float& r) {
-  const float g = held_to(__fmul_rn(sum, g_mul), 0x1p63f);
-  m = __fmaf_rn(ad.beta1, m, __fmul_rn(ad.omb1, g));
-  const float v = __fmaf_rn(__fmul_rn(ad.beta2, r), r, __fmul_rn(__fmul_rn(ad.omb2, g), g));
-  r = sqrt_approx(v);
-  const float upd = __fdividef(__fmul_rn(m, ad.inv_bc1), __fmaf_rn(r, ad.sbc2, ad.eps));
-  p = __fmaf_rn(-ad.lr, __fmaf_rn(ad.wd, p, upd), p);
+// The root of v >= 0 in the same way, from the approximate reciprocal root:
+// s = v * y, s + (v - s^2) * y / 2.  For v of 2^-100 and more; the root of
+// smaller ones is 2 units off at most, that of zero is zero.
+__device__ __forceinline__ float square_root(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 0x1p-126f)));
+  const float s = __fmul_rn(v, y);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), __fmul_rn(0.5f, y), s);
+}
+
+// max(|a|, |b|), NaN if either is.
+__device__ __forceinline__ float abs_max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 // A block's values in the registers of one warp, 8 a lane.
@@ -559,35 +602,103 @@ struct ListVals {
   float g[8], p[8], m[8], v[8];
 };
 
-// The update of a block, in place; with 8-bit moments m and v come as the
-// codes' values and leave as the values to be encoded, mc and vc are their
-// scales before and after.
-template <int STATES>
-__device__ __forceinline__ void list_update(ListVals& x, const AdamArgs& ad, float coef,
-                                            float g_mul, float& mc, float& vc) {
-  if constexpr (STATES == ZS_STATES_8BIT) {
-    uint32_t mtop = 0, vtop = 0;
+// What a CTA takes from the step's constants beside its tensor's multipliers.
+struct ListConsts {
+  float coef, g_mul;
+  ListRatios ratios;
+};
+
+// AdamW of a block with 8-bit moments: m and v come as the codes' values and
+// leave as the values to be encoded, mc and vc are their scales before and
+// after.  The new moments are those of adamw1 bit for bit, the update is as good:
+// the root of v_hat is taken as that of v, which is stored, times the bias
+// corrections' ratio.  Quotients and roots are the corrected ones above (with CUDA's
+// rounded division and root a step of the 124M-element list takes 506 us).  The
+// averaged gradient is held to +-2^63, where its square would leave fp32.
+__device__ __forceinline__ void list_update_q8(ListVals& x, const AdamArgs& ad,
+                                               const ListConsts& lc, float& mc, float& vc) {
+  if (lc.g_mul != 0.0f) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x.m[k] = __fmul_rn(x.m[k], mc);
-      x.v[k] = __fmul_rn(x.v[k], vc);
-      adamw1_q8(ad, g_mul, x.g[k], x.p[k], x.m[k], x.v[k]);
-      mtop = max(mtop, __float_as_uint(x.m[k]) & 0x7fffffffu);
-      vtop = max(vtop, __float_as_uint(x.v[k]) & 0x7fffffffu);
-    }
-    // (an inf or NaN has the largest bits: its block's scale is not finite)
-    mc = state_scale(__reduce_max_sync(0xffffffffu, mtop));
-    vc = state_scale(__reduce_max_sync(0xffffffffu, vtop));
-    const float mi = rcp_approx(mc), vi = rcp_approx(vc);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x.m[k] = __fmul_rn(x.m[k], mi);
-      const float q = __fmul_rn(x.v[k], vi);
-      x.v[k] = x.v[k] > 0.0f && q < 0x1p-9f ? 0x1p-9f : q;
-    }
+    for (int k = 0; k < 8; ++k) x.g[k] = __fmul_rn(x.g[k], lc.g_mul);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) adamw1<true>(ad, x.g[k], x.p[k], x.m[k], x.v[k], coef);
+    for (int k = 0; k < 8; ++k) x.g[k] = __fmul_rn(__fdiv_rn(x.g[k], ad.grad_div), lc.coef);
+  }
+  float mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float g = held_to(x.g[k], 0x1p63f);
+    const float r = __fmul_rn(x.v[k], vc);
+    x.m[k] = __fmaf_rn(ad.beta1, __fmul_rn(x.m[k], mc), __fmul_rn(ad.omb1, g));
+    x.v[k] = __fmaf_rn(ad.beta2, __fmul_rn(r, r), __fmul_rn(ad.omb2, __fmul_rn(g, g)));
+    mtop = abs_max_nan(mtop, x.m[k]);
+    vtop = abs_max_nan(vtop, x.v[k]);
+  }
+  // (an inf or NaN has the largest bits: its block's scale is not finite)
+  mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+  vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+  // Small blocks, scaled up by powers of two: a root below 2^-20 of its block's
+  // largest is stored as the least code, so the others are at least 2^-50.
+  float rs = 1.0f;
+  if (vtop < 0x1p-60f) {
+    rs = 0x1p-32f;
+    vtop = __fmul_rn(vtop, 0x1p64f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = __fmul_rn(x.v[k], 0x1p64f);
+  }
+  float cv = __fdiv_rn(__fsqrt_rn(vtop), 448.0f);
+  vc = __fmul_rn(cv, rs);
+  if (vc < 0x1p-126f) {
+    vc = 0x1p-126f;
+    cv = rs == 1.0f ? 0x1p-126f : 0x1p-94f;
+  }
+  const float root = __fmul_rn(lc.ratios.root, rs), root_lo = __fmul_rn(lc.ratios.root_lo, rs),
+              eps = lc.ratios.eps;
+  if (mtop <= 3.402823466e38f && vtop <= 3.402823466e38f && eps >= 0x1p-72f &&
+      eps <= 0x1p60f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float s = square_root(x.v[k]);
+      const float d = __fmaf_rn(s, root, __fmaf_rn(s, root_lo, eps));
+      const float upd = quotient(x.m[k], d, rcp_approx(d));
+      x.p[k] = __fmaf_rn(-ad.lr, __fmaf_rn(ad.wd, x.p[k], upd), x.p[k]);
+      x.v[k] = s;
+    }
+  } else {  // values that are not finite, or an eps that d could lie far from
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float s = __fsqrt_rn(x.v[k]);
+      float upd = __fdiv_rn(x.m[k], __fmaf_rn(s, root, __fmaf_rn(s, root_lo, eps)));
+      if (upd != upd) upd = 0.0f;  // as adamw1 has it
+      x.p[k] = __fmaf_rn(-ad.lr, __fmaf_rn(ad.wd, x.p[k], upd), x.p[k]);
+      x.v[k] = s;
+    }
+  }
+  mc = state_scale(__float_as_uint(mtop));
+  float cm = mc;
+  if (cm < 0x1p-60f) {
+    cm = __fmul_rn(cm, 0x1p64f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.m[k] = __fmul_rn(x.m[k], 0x1p64f);
+  }
+  const float mi = rcp_approx(cm), vi = rcp_approx(cv);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    x.m[k] = quotient(x.m[k], cm, mi);
+    const float q = quotient(x.v[k], cv, vi);
+    x.v[k] = x.v[k] > 0.0f && q < 0x1p-9f ? 0x1p-9f : q;
+  }
+}
+
+// The update of a block, in place.
+template <int STATES>
+__device__ __forceinline__ void list_update(ListVals& x, const AdamArgs& ad, const ListConsts& lc,
+                                            float& mc, float& vc) {
+  if constexpr (STATES == ZS_STATES_8BIT) {
+    list_update_q8(x, ad, lc, mc, vc);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) adamw1<true>(ad, x.g[k], x.p[k], x.m[k], x.v[k], lc.coef);
   }
 }
 
@@ -629,8 +740,8 @@ __device__ __forceinline__ void list_store8(const ListRec& rec, int64_t i0, cons
 // A block without the ring, for ragged ends and arrays off the 16-byte
 // boundary: n <= kBlockElems elements from `at` on, lane, lane + 32, ... of them.
 template <int STATES, int HT>
-__device__ __forceinline__ void list_block(const ListRec& rec, const AdamArgs& ad, float coef,
-                                           float g_mul, int64_t at, int n) {
+__device__ __forceinline__ void list_block(const ListRec& rec, const AdamArgs& ad,
+                                           const ListConsts& lc, int64_t at, int n) {
   const int lane = threadIdx.x & 31;
   uint8_t* const mq = static_cast<uint8_t*>(rec.m);
   uint8_t* const vq = static_cast<uint8_t*>(rec.v);
@@ -661,7 +772,7 @@ __device__ __forceinline__ void list_block(const ListRec& rec, const AdamArgs& a
     mc = rec.m_scale[blk];
     vc = rec.v_scale[blk];
   }
-  list_update<STATES>(x, ad, coef, g_mul, mc, vc);
+  list_update<STATES>(x, ad, lc, mc, vc);
   if constexpr (STATES == ZS_STATES_8BIT) {
     __syncwarp();  // every lane has read the block's scales
     if (lane == 0) {
@@ -779,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_list_apply(const ListPlan pl) {
   AdamArgs ad = pl.step->ad;
   ad.lr = __fmul_rn(ad.lr, rec.lr_mult);
   ad.wd = __fmul_rn(ad.wd, rec.wd_mult);
-  const float coef = pl.step->coef, g_mul = pl.step->g_mul;
+  const ListConsts lc = {pl.step->coef, pl.step->g_mul, pl.step->ratios};
   // the scales of this warp's block of unit u are kept by lane u
   static_assert(kListChunkUnits <= 32, "a lane for every unit of a chunk");
   float mcs = 0.0f, vcs = 0.0f;
@@ -802,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_list_apply(const ListPlan pl) {
       mc = __shfl_sync(0xffffffffu, mcs, u);
       vc = __shfl_sync(0xffffffffu, vcs, u);
     }
-    list_update<STATES>(x, ad, coef, g_mul, mc, vc);
+    list_update<STATES>(x, ad, lc, mc, vc);
     __syncwarp();  // the warp's reads of the stage come before the copies into it
     if (u + Ring::kStages < full)
       ring_fill<STATES>(stage, rec, i0 + (int64_t)(u + Ring::kStages) * kListUnit);
@@ -825,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_list_apply(const ListPlan pl) {
     const int64_t at = base + (int64_t)u * kListUnit + warp * kBlockElems;
     const int64_t n = rec.count - at;
     if (n <= 0) break;
-    list_block<STATES, HT>(rec, ad, coef, g_mul, at, n < kBlockElems ? (int)n : kBlockElems);
+    list_block<STATES, HT>(rec, ad, lc, at, n < kBlockElems ? (int)n : kBlockElems);
   }
 }
 
