@@ -714,7 +714,8 @@ zs_status zs_tensors_apply(zs_tensors* t, const int32_t* d_flag, const double* d
  * of `cols` elements, in fp32 from the loaded halves on:
  *   h = x (+ residual)                    sum_out = RNE(h)
  *   rstd = 1 / sqrt(mean(h^2) + eps)
- *   y = h * rstd * weight                 out = RNE(y), or E4M3(y / c) with
+ *   y = h * rstd * weight                 out = RNE(y), or E4M3(y / c), the value
+ *                                         nearest to the fp32 quotient, with
  *                                         c = max|y| / 448 (at least 2^-126)
  * over the whole row (group 0) or over each `group` columns (32, 64 or 128;
  * the last may be shorter).  y is formed from h before its rounding into

@@ -446,10 +446,8 @@ __launch_bounds__(MAXT, MAXT == 512 && ACC == kShifted ? 2
           c = e4m3_scale(abs_bits(top));
           if (e < cols && (e & (a.group - 1)) == 0) scales[e >> a.group_log2] = c;
         }
-        const float inv = rcp_approx(c);
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(h[k][i], inv);
+        float (&q)[8] = h[k];
+        by_scale(q, c);
         if (norm_whole<ACC>(ring.bits, k, cols)) {
           *reinterpret_cast<uint2*>(out + e) = pack8_e4m3(q);
         } else if (ACC == kShifted && norm_live<ACC>(ring.bits, k, cols)) {
@@ -471,7 +469,9 @@ __launch_bounds__(MAXT, MAXT == 512 && ACC == kShifted ? 2
               c = e4m3_scale(top);
               if ((e & (a.group - 1)) == 0) scales[e >> a.group_log2] = c;
             }
-            out[e] = (uint8_t)float2_to_e4m3x2(__fmul_rn(h[k][i], rcp_approx(c)), 0.0f);
+            float q[1] = {h[k][i]};
+            by_scale(q, c);
+            out[e] = (uint8_t)float2_to_e4m3x2(q[0], 0.0f);
           }
         }
       }
@@ -549,12 +549,15 @@ __global__ void __launch_bounds__(1024) k_norm_wide(const __grid_constant__ Norm
       if (e < cols) {
         if (a.sum != nullptr)
           a.sum[row * a.sum_stride + e] = (uint16_t)float_to_half_bits<DT>(h);
-        if constexpr (OUT != kOutHalf)
+        if constexpr (OUT != kOutHalf) {
+          float q[1] = {y};
+          by_scale(q, c);
           static_cast<uint8_t*>(a.out)[row * a.out_stride + e] =
-              (uint8_t)float2_to_e4m3x2(__fmul_rn(y, rcp_approx(c)), 0.0f);
-        else
+              (uint8_t)float2_to_e4m3x2(q[0], 0.0f);
+        } else {
           static_cast<uint16_t*>(a.out)[row * a.out_stride + e] =
               (uint16_t)float_to_half_bits<DT>(y);
+        }
       }
     }
   }

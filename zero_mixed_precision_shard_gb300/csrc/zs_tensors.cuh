@@ -544,20 +544,6 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float a[8]) {
                     float2_to_e4m3x2(a[4], a[5]) | (float2_to_e4m3x2(a[6], a[7]) << 16));
 }
 
-// The scale of values whose largest magnitude has these fp32 bits: at least
-// 2^-126, so that its reciprocal is finite; inf and NaN stay.
-__device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
-  const float c = __fmul_rn(__uint_as_float(amax_bits), 1.0f / 448.0f);
-  return c < 0x1p-126f ? 0x1p-126f : c;
-}
-
-// The scale of a block of moments, as above with the quotient rounded once: the
-// state goes from step to step through it.
-__device__ __forceinline__ float state_scale(uint32_t amax_bits) {
-  const float c = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
-  return c < 0x1p-126f ? 0x1p-126f : c;
-}
-
 // x held to +-limit; a NaN stays one.
 __device__ __forceinline__ float held_to(float x, float limit) {
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-limit));
@@ -578,6 +564,32 @@ __device__ __forceinline__ float rcp_approx(float c) {
 __device__ __forceinline__ float quotient(float x, float c, float rcp) {
   const float q = __fmul_rn(x, rcp);
   return __fmaf_rn(__fmaf_rn(-q, c, x), rcp, q);
+}
+
+// top / 448 rounded (a quotient by 7 lies a fourteenth of a unit from any midpoint
+// or more, so the corrected one is it); inf and NaN stay.
+__device__ __forceinline__ float over_448(float top) {
+  const float c = quotient(top, 448.0f, 1.0f / 448.0f);
+  return top <= 3.402823466e38f ? c : top;
+}
+
+// The scale of values whose largest magnitude has these fp32 bits.
+__device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
+  const float c = over_448(__uint_as_float(amax_bits));
+  return c < 0x1p-126f ? 0x1p-126f : c;
+}
+
+// Values by their scale, ready for E4M3 (small scales brought up, exactly).
+template <int N>
+__device__ __forceinline__ void by_scale(float (&x)[N], float c) {
+  if (c < 0x1p-60f) {
+    c = __fmul_rn(c, 0x1p64f);
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = __fmul_rn(x[k], 0x1p64f);
+  }
+  const float r = rcp_approx(c);
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = quotient(x[k], c, r);
 }
 
 // The root of v >= 0 in the same way, from the approximate reciprocal root:
@@ -646,7 +658,7 @@ __device__ __forceinline__ void list_update_q8(ListVals& x, const AdamArgs& ad,
 #pragma unroll
     for (int k = 0; k < 8; ++k) x.v[k] = __fmul_rn(x.v[k], 0x1p64f);
   }
-  float cv = __fdiv_rn(__fsqrt_rn(vtop), 448.0f);
+  float cv = over_448(square_root(vtop));
   vc = __fmul_rn(cv, rs);
   if (vc < 0x1p-126f) {
     vc = 0x1p-126f;
@@ -674,17 +686,11 @@ __device__ __forceinline__ void list_update_q8(ListVals& x, const AdamArgs& ad,
       x.v[k] = s;
     }
   }
-  mc = state_scale(__float_as_uint(mtop));
-  float cm = mc;
-  if (cm < 0x1p-60f) {
-    cm = __fmul_rn(cm, 0x1p64f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x.m[k] = __fmul_rn(x.m[k], 0x1p64f);
-  }
-  const float mi = rcp_approx(cm), vi = rcp_approx(cv);
+  mc = e4m3_scale(__float_as_uint(mtop));
+  by_scale(x.m, mc);
+  const float vi = rcp_approx(cv);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    x.m[k] = quotient(x.m[k], cm, mi);
     const float q = quotient(x.v[k], cv, vi);
     x.v[k] = x.v[k] > 0.0f && q < 0x1p-9f ? 0x1p-9f : q;
   }
