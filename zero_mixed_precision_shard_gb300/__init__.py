@@ -98,6 +98,10 @@ class zs_norm_shape(ctypes.Structure):
                 ("sum_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
                 ("dy_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64)]
 
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        self.__dict__.pop("holds", None)  # made anew (see _norm_holds)
+
 
 def _load():
     if not os.path.exists(LIB_PATH):
@@ -260,6 +264,7 @@ class Ctx:
         if rc != ZS_OK:
             raise ZsError(rc, "zs_ctx_create failed")
         self.handle = h
+        self.work_bytes = {}  # zs_rmsnorm_bwd_work by the bytes of the rows and the weight
 
     def check(self, rc: int):
         if rc != ZS_OK:
@@ -635,21 +640,108 @@ class Engine:
             pass
 
 
+# What the list step and the norm take from a tensor is checked before its
+# address is: the element's format, that the elements lie one after the other (an
+# expanded gradient does not), and that there are enough of them.  Plain addresses
+# (int) are the caller's own.
+
+_FORMATS = {}
+
+
+class _Any(tuple):
+    """Every format."""
+
+    def __contains__(self, dtype):
+        return True
+
+
+_ANY = _Any()
+
+
+def _formats():
+    """Tensor formats by what an argument holds; halves also as bit patterns."""
+    if not _FORMATS:
+        import torch
+        bits = (torch.int16, torch.uint16)
+        _FORMATS.update({ZS_FP16: (torch.float16,) + bits, ZS_BF16: (torch.bfloat16,) + bits,
+                         ZS_FP32: (torch.float32,),
+                         "codes": (torch.float8_e4m3fn, torch.uint8, torch.int8),
+                         "flag": (torch.int32,), "sum": (torch.float64,)})
+    return _FORMATS
+
+
+def _misfit(t, name, formats, nbytes):
+    """Why a tensor does not hold nbytes of contiguous elements; None: it does."""
+    if t is None or isinstance(t, int) or not hasattr(t, "dtype"):
+        return None
+    if t.dtype not in formats:
+        return f"{name} is {t.dtype}, not {formats[0]}"
+    if not t.is_contiguous():
+        return f"{name} is not contiguous"
+    if t.nbytes < nbytes:
+        return f"{name} holds {t.nbytes} bytes, {nbytes} are needed"
+    return None
+
+
+def _fitting(t, name, formats, nbytes):
+    """The address of a tensor that holds nbytes of contiguous elements."""
+    try:
+        if t.dtype in formats and t.nbytes >= nbytes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # None, an address, an object with an address alone
+        return _addr(t)
+    raise ZsError(ZS_ERR_ARG, _misfit(t, name, formats, nbytes))
+
+
+def _rows(t, name, formats, rows, cols, stride):
+    """The address of a tensor that holds `rows` rows of `cols` elements,
+    `stride` elements apart (0: cols)."""
+    if t is None or isinstance(t, int) or not hasattr(t, "dtype"):
+        return _addr(t)
+    size = t.element_size()
+    if stride == 0 or stride == cols:
+        return _fitting(t, name, formats, rows * cols * size)
+    if t.dtype not in formats:
+        raise ZsError(ZS_ERR_ARG, _misfit(t, name, formats, 0))
+    have = t.untyped_storage().nbytes() - t.storage_offset() * size
+    need = ((rows - 1) * stride + cols) * size if rows > 0 else 0
+    if have < need:
+        raise ZsError(ZS_ERR_ARG, f"{name} has {have} bytes from its first element on, its rows "
+                                  f"reach over {need}")
+    if t.shape == (rows, cols) and rows > 1 and (
+            t.stride(0) != stride or (cols > 1 and t.stride(1) != 1)):
+        raise ZsError(ZS_ERR_ARG, f"{name} has strides {t.stride()}, the shape's is {stride}")
+    return t.data_ptr()
+
+
 def make_tensor(grad, master, m, v, half_out=None, m_scale=None, v_scale=None,
                 lr_mult: float = 1.0, wd_mult: float = 1.0, count: int | None = None,
                 grad_dtype=None) -> zs_tensor:
     """One entry of a TensorList.  count and grad_dtype default to the master's
-    number of elements and the gradient's format (torch tensors, contiguous)."""
-    for name, t in (("grad", grad), ("master", master), ("m", m), ("v", v),
-                    ("half_out", half_out), ("m_scale", m_scale), ("v_scale", v_scale)):
-        if hasattr(t, "is_contiguous") and not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
+    number of elements and the gradient's format (torch tensors, contiguous).
+    Raises ValueError where a tensor's format or size does not fit."""
     if count is None:
         count = master.numel()
     if grad_dtype is None:
         grad_dtype = ZS_FP32 if str(grad.dtype) == "torch.float32" else _dtype(grad.dtype)
-    return zs_tensor(_addr(grad), _addr(master), _addr(m), _addr(v), _addr(m_scale),
-                     _addr(v_scale), _addr(half_out), count, grad_dtype, lr_mult, wd_mult, 0)
+    formats = _formats()
+    fp32, moments = formats[ZS_FP32], formats[ZS_FP32] + formats["codes"]
+    blocks = 4 * -(-count // ZS_STATE_BLOCK)
+    for name, t, held, each in (
+            ("grad", grad, formats.get(grad_dtype, _ANY), (4 if grad_dtype == ZS_FP32 else 2) * count),
+            ("master", master, fp32, 4 * count),
+            ("m", m, moments, getattr(m, "itemsize", 1) * count),
+            ("v", v, moments, getattr(v, "itemsize", 1) * count),
+            ("half_out", half_out, formats[ZS_FP16] + formats[ZS_BF16], 2 * count),
+            ("m_scale", m_scale, fp32, blocks), ("v_scale", v_scale, fp32, blocks)):
+        why = _misfit(t, name, held, each)
+        if why is not None:
+            raise ValueError(why)
+    e = zs_tensor(_addr(grad), _addr(master), _addr(m), _addr(v), _addr(m_scale),
+                  _addr(v_scale), _addr(half_out), count, grad_dtype, lr_mult, wd_mult, 0)
+    # what only the list can compare (see TensorList)
+    e.formats = tuple(getattr(t, "dtype", None) for t in (m, v, half_out))
+    return e
 
 
 class TensorList:
@@ -660,9 +752,24 @@ class TensorList:
         self.handle = ctypes.c_void_p()
         self.ctx = ctx
         self.n = len(entries)
+        self._check(entries, _dtype(dt), states)
+        self.grads = [(e.grad_dtype, e.count) for e in entries]
         arr = (zs_tensor * max(1, self.n))(*entries)
         ctx.check(lib.zs_tensors_create(ctx.handle, arr, self.n, _dtype(dt), states,
                                         ctypes.byref(self.handle)))
+
+    @staticmethod
+    def _check(entries, dt, states):
+        """The moments' and half copies' formats against the list's."""
+        formats = _formats()
+        moments = {ZS_STATES_FP32: formats[ZS_FP32], ZS_STATES_8BIT: formats["codes"]}.get(states)
+        for i, e in enumerate(entries):
+            m, v, half = getattr(e, "formats", (None, None, None))
+            for name, held in (("m", m), ("v", v)):
+                if held is not None and moments is not None and held not in moments:
+                    raise ZsError(ZS_ERR_ARG, f"tensor {i}: {name} is {held}, not {moments[0]}")
+            if half is not None and dt in (ZS_FP16, ZS_BF16) and half not in formats[dt]:
+                raise ZsError(ZS_ERR_DTYPE, f"tensor {i}: half_out is {half}, not {formats[dt][0]}")
 
     def close(self):
         if self.handle:
@@ -677,29 +784,41 @@ class TensorList:
 
 
 def zs_tensors_set_grads(tensors: TensorList, grads, stream=None):
+    """grads: tensors (or addresses), one per tensor of the list, in the formats
+    given at creation; ValueError where one does not fit.  An array made by
+    pointer_array holds addresses alone."""
     if len(grads) != tensors.n:
         raise ValueError(f"{len(grads)} gradients for {tensors.n} tensors")
+    if not isinstance(grads, ctypes.Array):
+        formats = _formats()
+        for i, (g, (dt, count)) in enumerate(zip(grads, tensors.grads)):
+            why = _misfit(g, f"gradient {i}", formats[dt], (4 if dt == ZS_FP32 else 2) * count)
+            if why is not None:
+                raise ValueError(why)
     tensors.ctx.check(lib.zs_tensors_set_grads(tensors.handle, _ptrs(grads), _stream(stream)))
 
 
 def zs_tensors_step_async(tensors: TensorList, n: int, accum_steps: int, hp: zs_adam_hparams,
                           sched, max_norm: float, d_state, d_grad_norm=None, stream=None):
+    norm = _fitting(d_grad_norm, "d_grad_norm", _formats()[ZS_FP32], 4)
     tensors.ctx.check(lib.zs_tensors_step_async(
         tensors.handle, n, accum_steps, ctypes.byref(hp),
         ctypes.byref(sched) if sched is not None else None, max_norm, _addr(d_state),
-        _addr(d_grad_norm), _stream(stream)))
+        norm, _stream(stream)))
 
 
 def zs_tensors_check(tensors: TensorList, grad_div: float, d_flag, d_sumsq=None, stream=None):
-    tensors.ctx.check(lib.zs_tensors_check(tensors.handle, grad_div, _addr(d_flag),
-                                           _addr(d_sumsq), _stream(stream)))
+    f = _formats()
+    flag, total = _fitting(d_flag, "d_flag", f["flag"], 4), _fitting(d_sumsq, "d_sumsq", f["sum"], 8)
+    tensors.ctx.check(lib.zs_tensors_check(tensors.handle, grad_div, flag, total, _stream(stream)))
 
 
 def zs_tensors_apply(tensors: TensorList, d_flag, d_sumsq, max_norm: float, grad_div: float,
                      hp: zs_adam_hparams, step: int, stream=None):
-    tensors.ctx.check(lib.zs_tensors_apply(tensors.handle, _addr(d_flag), _addr(d_sumsq),
-                                           max_norm, grad_div, ctypes.byref(hp), step,
-                                           _stream(stream)))
+    f = _formats()
+    flag, total = _fitting(d_flag, "d_flag", f["flag"], 4), _fitting(d_sumsq, "d_sumsq", f["sum"], 8)
+    tensors.ctx.check(lib.zs_tensors_apply(tensors.handle, flag, total, max_norm, grad_div,
+                                           ctypes.byref(hp), step, _stream(stream)))
 
 
 def make_norm_shape(rows: int, cols: int, dt, eps: float, bits: int = 16, group: int = 0,
@@ -710,11 +829,45 @@ def make_norm_shape(rows: int, cols: int, dt, eps: float, bits: int = 16, group:
                          sum_stride, out_stride, dy_stride, dx_stride)
 
 
+def _norm_holds(shape):
+    """What a shape's arrays hold, made once per shape: formats of the halves, the
+    output and fp32; bytes of the rows in halves, of the output, the scales, a value
+    per row and the weight; whether the rows of the norm and of its gradients are
+    contiguous; and the shape's reference."""
+    f, rows, cols = _formats(), shape.rows, shape.cols
+    half, q8 = f.get(shape.dt, ()), shape.bits == 8
+    if shape.dt not in (ZS_FP16, ZS_BF16):  # (for the library to refuse)
+        half = f[ZS_FP16] + f[ZS_BF16] + f[ZS_FP32]
+    groups = -(-cols // shape.group) if shape.group > 0 else 1
+    whole = [s in (0, cols) for s in (shape.x_stride, shape.residual_stride, shape.sum_stride,
+                                      shape.out_stride, shape.dy_stride, shape.dx_stride)]
+    holds = (half, f["codes"] if q8 else half, f[ZS_FP32], 2 * rows * cols,
+             rows * cols * (1 if q8 else 2), 4 * rows * groups, 4 * rows, 2 * cols,
+             all(whole[:4]), whole[0] and whole[1] and whole[4] and whole[5], ctypes.byref(shape))
+    shape.__dict__["holds"] = holds
+    return holds
+
+
 def zs_rmsnorm(ctx: Ctx, shape: zs_norm_shape, x, residual, weight, sum_out, out, scales=None,
                rstd=None, stream=None):
-    ctx.check(lib.zs_rmsnorm(ctx.handle, ctypes.byref(shape), _addr(x), _addr(residual),
-                             _addr(weight), _addr(sum_out), _addr(out), _addr(scales),
-                             _addr(rstd), _stream(stream)))
+    """Tensors that do not hold what the shape says are refused with ZS_ERR_ARG."""
+    half, codes, fp32, n, n_out, n_scales, n_rows, n_weight, plain, _, ref = (
+        shape.__dict__.get("holds") or _norm_holds(shape))
+    if plain:
+        a = (_fitting(x, "x", half, n), _fitting(residual, "residual", half, n))
+        b = (_fitting(sum_out, "sum_out", half, n), _fitting(out, "out", codes, n_out))
+    else:
+        rows, cols = shape.rows, shape.cols
+        a = (_rows(x, "x", half, rows, cols, shape.x_stride),
+             _rows(residual, "residual", half, rows, cols, shape.residual_stride))
+        b = (_rows(sum_out, "sum_out", half, rows, cols, shape.sum_stride),
+             _rows(out, "out", codes, rows, cols, shape.out_stride))
+    rc = lib.zs_rmsnorm(ctx.handle, ref, *a, _fitting(weight, "weight", half, n_weight), *b,
+                        _fitting(scales, "scales", fp32, n_scales),
+                        _fitting(rstd, "rstd", fp32, n_rows),
+                        _current_stream() if stream is None else _stream(stream))
+    if rc:
+        ctx.check(rc)
 
 
 def zs_rmsnorm_bwd_work(ctx: Ctx, shape: zs_norm_shape) -> int:
@@ -726,10 +879,28 @@ def zs_rmsnorm_bwd_work(ctx: Ctx, shape: zs_norm_shape) -> int:
 
 def zs_rmsnorm_bwd(ctx: Ctx, shape: zs_norm_shape, dy, h, rstd, weight, dsum, dx, dweight, work,
                    accumulate: bool = False, stream=None):
-    ctx.check(lib.zs_rmsnorm_bwd(ctx.handle, ctypes.byref(shape), _addr(dy), _addr(h),
-                                 _addr(rstd), _addr(weight), _addr(dsum), _addr(dx),
-                                 _addr(dweight), 1 if accumulate else 0, _addr(work),
-                                 _stream(stream)))
+    """Tensors that do not hold what the shape says are refused with ZS_ERR_ARG."""
+    half, _, fp32, n, _, _, n_rows, n_weight, _, plain, ref = (
+        shape.__dict__.get("holds") or _norm_holds(shape))
+    if plain:
+        a = (_fitting(dy, "dy", half, n), _fitting(h, "h", half, n))
+        b = (_fitting(dsum, "dsum", half, n), _fitting(dx, "dx", half, n))
+    else:
+        rows, cols = shape.rows, shape.cols
+        a = (_rows(dy, "dy", half, rows, cols, shape.dy_stride),
+             _rows(h, "h", half, rows, cols, shape.x_stride))
+        b = (_rows(dsum, "dsum", half, rows, cols, shape.residual_stride),
+             _rows(dx, "dx", half, rows, cols, shape.dx_stride))
+    need = ctx.work_bytes.get((n, n_weight))  # (rows and columns, in bytes)
+    if need is None and hasattr(work, "nbytes"):
+        need = ctx.work_bytes[n, n_weight] = zs_rmsnorm_bwd_work(ctx, shape)
+    rc = lib.zs_rmsnorm_bwd(ctx.handle, ref, *a, _fitting(rstd, "rstd", fp32, n_rows),
+                            _fitting(weight, "weight", half, n_weight), *b,
+                            _fitting(dweight, "dweight", fp32, 2 * n_weight),
+                            1 if accumulate else 0, _fitting(work, "work", _ANY, need),
+                            _current_stream() if stream is None else _stream(stream))
+    if rc:
+        ctx.check(rc)
 
 
 def zs_copy_peak(ctx: Ctx, src, dst, nbytes: int, read_only: bool = False, stream=None):
