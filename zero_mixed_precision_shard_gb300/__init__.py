@@ -832,8 +832,8 @@ def make_norm_shape(rows: int, cols: int, dt, eps: float, bits: int = 16, group:
 def _norm_holds(shape):
     """What a shape's arrays hold, made once per shape: formats of the halves, the
     output and fp32; bytes of the rows in halves, of the output, the scales, a value
-    per row and the weight; whether the rows of the norm and of its gradients are
-    contiguous; and the shape's reference."""
+    per row and the weight; and whether the rows of the norm and of its gradients are
+    contiguous."""
     f, rows, cols = _formats(), shape.rows, shape.cols
     half, q8 = f.get(shape.dt, ()), shape.bits == 8
     if shape.dt not in (ZS_FP16, ZS_BF16):  # (for the library to refuse)
@@ -843,7 +843,7 @@ def _norm_holds(shape):
                                       shape.out_stride, shape.dy_stride, shape.dx_stride)]
     holds = (half, f["codes"] if q8 else half, f[ZS_FP32], 2 * rows * cols,
              rows * cols * (1 if q8 else 2), 4 * rows * groups, 4 * rows, 2 * cols,
-             all(whole[:4]), whole[0] and whole[1] and whole[4] and whole[5], ctypes.byref(shape))
+             all(whole[:4]), whole[0] and whole[1] and whole[4] and whole[5])
     shape.__dict__["holds"] = holds
     return holds
 
@@ -851,7 +851,7 @@ def _norm_holds(shape):
 def zs_rmsnorm(ctx: Ctx, shape: zs_norm_shape, x, residual, weight, sum_out, out, scales=None,
                rstd=None, stream=None):
     """Tensors that do not hold what the shape says are refused with ZS_ERR_ARG."""
-    half, codes, fp32, n, n_out, n_scales, n_rows, n_weight, plain, _, ref = (
+    half, codes, fp32, n, n_out, n_scales, n_rows, n_weight, plain, _ = (
         shape.__dict__.get("holds") or _norm_holds(shape))
     if plain:
         a = (_fitting(x, "x", half, n), _fitting(residual, "residual", half, n))
@@ -862,7 +862,8 @@ def zs_rmsnorm(ctx: Ctx, shape: zs_norm_shape, x, residual, weight, sum_out, out
              _rows(residual, "residual", half, rows, cols, shape.residual_stride))
         b = (_rows(sum_out, "sum_out", half, rows, cols, shape.sum_stride),
              _rows(out, "out", codes, rows, cols, shape.out_stride))
-    rc = lib.zs_rmsnorm(ctx.handle, ref, *a, _fitting(weight, "weight", half, n_weight), *b,
+    rc = lib.zs_rmsnorm(ctx.handle, ctypes.byref(shape), *a,
+                        _fitting(weight, "weight", half, n_weight), *b,
                         _fitting(scales, "scales", fp32, n_scales),
                         _fitting(rstd, "rstd", fp32, n_rows),
                         _current_stream() if stream is None else _stream(stream))
@@ -880,7 +881,7 @@ def zs_rmsnorm_bwd_work(ctx: Ctx, shape: zs_norm_shape) -> int:
 def zs_rmsnorm_bwd(ctx: Ctx, shape: zs_norm_shape, dy, h, rstd, weight, dsum, dx, dweight, work,
                    accumulate: bool = False, stream=None):
     """Tensors that do not hold what the shape says are refused with ZS_ERR_ARG."""
-    half, _, fp32, n, _, _, n_rows, n_weight, _, plain, ref = (
+    half, _, fp32, n, _, _, n_rows, n_weight, _, plain = (
         shape.__dict__.get("holds") or _norm_holds(shape))
     if plain:
         a = (_fitting(dy, "dy", half, n), _fitting(h, "h", half, n))
@@ -894,7 +895,8 @@ def zs_rmsnorm_bwd(ctx: Ctx, shape: zs_norm_shape, dy, h, rstd, weight, dsum, dx
     need = ctx.work_bytes.get((n, n_weight))  # (rows and columns, in bytes)
     if need is None and hasattr(work, "nbytes"):
         need = ctx.work_bytes[n, n_weight] = zs_rmsnorm_bwd_work(ctx, shape)
-    rc = lib.zs_rmsnorm_bwd(ctx.handle, ref, *a, _fitting(rstd, "rstd", fp32, n_rows),
+    rc = lib.zs_rmsnorm_bwd(ctx.handle, ctypes.byref(shape), *a,
+                            _fitting(rstd, "rstd", fp32, n_rows),
                             _fitting(weight, "weight", half, n_weight), *b,
                             _fitting(dweight, "dweight", fp32, 2 * n_weight),
                             1 if accumulate else 0, _fitting(work, "work", _ANY, need),
