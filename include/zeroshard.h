@@ -146,8 +146,9 @@ zs_status zs_scaler_init(zs_scaler* s, float scale, float min_scale, int32_t win
  * flag (a device int32, zero at creation), a result word in mapped pinned
  * host memory (the update kernel writes the step's flag and new scale there;
  * the synchronising calls read it after the stream sync, with no copy), 8 MB
- * of scratch for the clipping norm's per-CTA partial sums (sized here, so no
- * later call allocates device memory), a pinned mirror of the norm, and the
+ * of scratch for the clipping norm's per-CTA partial sums (sized here, so that of
+ * the later calls only zs_tensors_create allocates device memory), a pinned mirror
+ * of the norm, and the
  * fused step's grid barrier (16 device bytes) with its timeout word (mapped
  * pinned).  Environment: ZEROSHARD_PDL=0 launches the step's kernels without
  * programmatic dependent launch; ZEROSHARD_FUSED=0 starts the context with

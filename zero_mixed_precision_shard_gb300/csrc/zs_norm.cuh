@@ -325,9 +325,27 @@ struct NormRing {
   }
 };
 
-// Threads an SM that the norm's grid aims at, and that the registers of its
-// gradients are given out for.  (With whole lines and two units 512 are faster
-// than 1,024, 81 against 89 us for 8192 x 8192, for the reason above.)
+// Threads an SM that the norm's grid aims at, and that its registers are given
+// out for: more of them hide more latency, fewer spill less and keep the rows in
+// flight together.  Each against a step fewer and a step more, us for 64 million
+// bf16 elements with residual, 16 bits out (fewer / taken / more):
+//   whole lines    1 unit, 256 columns: 84 / 85 / 90 with 768, 1,024 and 1,536
+//                  2 units, 4,096: 93 / 80 / 84 with 256, 512 and 1,024
+//                  3 units, 768: 83 / 87 / 92 with 512, 768 and 1,024 (79 / 75 / 79 to 8 bits)
+//                  4 units, 1,024: 82 / 83 / 90 with 384, 512 and 768
+//   shifted rows   1 unit, 250: 134 / 135 / 153 with 768, 1,024 and 1,536
+//                  2 units, 2,047: 92 / 86 / 98 with 512, 768 and 1,024
+//                  3 units, 763: 120 / 92 / 92 with 384, 512 and 768
+//                  4 units, 1,001: 98 / 88 / 91 with 256, 384 and 512
+//   elements       1 unit, 1,000: 294 / 190 / 164 with 512, 768 and 1,024
+//                  2 units, 4,096: 448 / 248 / 186 with 256, 512 and 768
+// (One unit of whole lines would be faster with fewer where several warps share a
+// row, 1,280 columns 78 / 88 / 91, and single elements with more.)  The gradients:
+//   1 unit         lines, 256: 79 / 88 / 132 with 768, 1,024 and 1,536;
+//                  shifted, 250: 238 / 166 / 299 with 512, 768 and 1,024
+//   2 units        4,096: 94 / 81 / 122 with 256, 512 and 768; 2,047: 236 / 124 / 197
+//   3 and 4        768: 79 / 79 / 100 with 256, 384 and 512; 763: 136 / 116 / 298;
+//                  1,024: 80 / 82 / 85; 1,001: 109 / 95 / 240
 __host__ __device__ constexpr int norm_sm_threads(int u, int acc) {
   return acc == kLines     ? (u == 1 ? 1024 : u == 2 ? 512 : u == 3 ? 768 : 512)
          : acc == kShifted ? (u == 1 ? 1024 : u == 2 ? 768 : u == 3 ? 512 : 384)
@@ -337,6 +355,8 @@ __host__ __device__ constexpr int norm_bwd_sm_threads(int u, int acc) {
   return u == 1 ? (acc == kShifted ? 768 : 1024) : u == 2 ? 512 : 384;
 }
 
+// (Shifted rows of up to 512 threads are held to 64 registers for two CTAs an SM:
+// 4,095 columns 107 us, 126 with one.)
 template <int DT, int U, int OUT, int ACC, int MAXT>
 __global__ void
 __launch_bounds__(MAXT, MAXT == 512 && ACC == kShifted ? 2
@@ -586,6 +606,8 @@ __device__ __forceinline__ float cluster_load(uint32_t at, int rank) {
   return x;
 }
 
+// (257 to 320 threads are a form of their own, two CTAs an SM at 102 registers: rows
+// of 4,095 columns 123 us for 64 million elements, 145 among those of up to 512.)
 template <int DT, int U, int ACC, int MAXT>
 __global__ void
 __launch_bounds__(MAXT, MAXT == 320 ? 2 : MAXT <= 512 ? norm_bwd_sm_threads(U, ACC) / MAXT : 1)
@@ -618,8 +640,11 @@ __launch_bounds__(MAXT, MAXT == 320 ? 2 : MAXT <= 512 ? norm_bwd_sm_threads(U, A
     const float rstd_next = row + at.step < a.rows ? a.rstd[row + at.step] : 0.0f;
     // Where the registers run short a row is taken from the ring a second time
     // for dx instead of being held; the slot is filled again only after that.
-    // (60000 x 1001: 89 us, 163 held; 32768 x 1024 48 and 61; but 8192 x 8192
-    // 88 and 86, 32768 x 768 38 and 37.)
+    // (us for 64 million elements, taken twice and held: lines of 1,024 columns 82
+    // and 105, 16,384 121 and 166; shifted rows of 763 116 and 212, 1,001 95 and
+    // 172, 2,047 124 and 140, 4,095 123 and 190, 8,191 231 and 278; but lines of 768
+    // 80 and 79, 8,192 85 and 83, shifted rows of 1,211 124 and 112, single
+    // elements of 1,000 251 and 197.)
     constexpr bool kTwice =
         U == 4 || (U == 3 && ACC == kShifted) ||
         (U == 2 && (MAXT > 512 || MAXT == 320 || ACC == kShifted));

@@ -10,7 +10,8 @@
 //
 // Both are bound by HBM (measured at 124M elements: the update moves 28 bytes
 // an element with fp16 gradients and 32-bit moments at 6.9 TB/s, 504 us, and 16
-// with 8-bit ones at 6.4 TB/s, 310 us; the check reads 2 at 5.9 TB/s).
+// with 8-bit ones at 6.6 TB/s, 304 us; the check reads 2 at 5.2 TB/s, 48 us with
+// its fixed start and end, and at 5.9 over 1.07 GB).
 //
 // The update's CTA takes one chunk of one tensor (the plan's chunk table, built
 // at creation), a warp a block of 256 elements at a time: through a ring of
@@ -424,8 +425,8 @@ __device__ __forceinline__ void list_finish(const ListPlan& pl, const ListFinish
 // each thread copies its words of the batches ahead into a ring in shared
 // memory that it reads alone.  (A CTA per chunk instead pays the end of a CTA --
 // its sum, the fence, the count of finished CTAs, about a microsecond -- for
-// every chunk: 73 us for 124M fp16 gradients, 53 so, 5.9 TB/s beside a fixed 10 us;
-// a kernel that only reads reaches 6.66.)
+// every chunk: 73 us for 124M fp16 gradients, 48 so; a kernel that only reads
+// reaches 6.66 TB/s.)
 constexpr int kCheckStages = 3;
 template <int HT>
 __global__ void __launch_bounds__(kThreads, kListCheckCtas)
@@ -624,9 +625,9 @@ struct ListConsts {
 // leave as the values to be encoded, mc and vc are their scales before and
 // after.  The new moments are those of adamw1 bit for bit, the update is as good:
 // the root of v_hat is taken as that of v, which is stored, times the bias
-// corrections' ratio.  Quotients and roots are the corrected ones above (with CUDA's
-// rounded division and root a step of the 124M-element list takes 506 us).  The
-// averaged gradient is held to +-2^63, where its square would leave fp32.
+// corrections' ratio.  Quotients and roots are the corrected ones above (a step of
+// the 124M-element list takes 353 us, 506 with CUDA's rounded division and root).
+// The averaged gradient is held to +-2^63, where its square would leave fp32.
 __device__ __forceinline__ void list_update_q8(ListVals& x, const AdamArgs& ad,
                                                const ListConsts& lc, float& mc, float& vc) {
   if (lc.g_mul != 0.0f) {
@@ -650,7 +651,9 @@ __device__ __forceinline__ void list_update_q8(ListVals& x, const AdamArgs& ad,
   mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
   vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
   // Small blocks, scaled up by powers of two: a root below 2^-20 of its block's
-  // largest is stored as the least code, so the others are at least 2^-50.
+  // largest is stored as the least code, so the others are at least 2^-50.  (To
+  // the update such a root, 2 units off at most, is nothing beside an eps of
+  // 2^-48 or more.)
   float rs = 1.0f;
   if (vtop < 0x1p-60f) {
     rs = 0x1p-32f;
