@@ -213,7 +213,7 @@ def test_norm_strides_that_do_not_fit(zs):
 
 def test_workspace_that_does_not_fit(zs):
     ctx = NoCtx()
-    ctx.work_bytes[2 * ROWS * COLS, 2 * COLS] = 320
+    ctx.work_bytes[ROWS, COLS] = 320
     with pytest.raises(Reached):
         run(zs, backward_args(work=torch.zeros(320, dtype=torch.uint8)), ctx=ctx)
     with pytest.raises(Reached):

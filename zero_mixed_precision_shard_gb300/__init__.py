@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 from ._build import HEADER, LIB_PATH, SOURCES, build, build_cmd  # noqa: F401,E402
@@ -101,6 +102,11 @@ class zs_norm_shape(ctypes.Structure):
     def __setattr__(self, name, value):
         super().__setattr__(name, value)
         self.__dict__.pop("holds", None)  # made anew (see _norm_holds)
+
+
+# its fields at once, without an assignment each
+_NORM_SHAPE = struct.Struct("=qqiiif6q")
+assert _NORM_SHAPE.size == ctypes.sizeof(zs_norm_shape)
 
 
 def _load():
@@ -264,7 +270,7 @@ class Ctx:
         if rc != ZS_OK:
             raise ZsError(rc, "zs_ctx_create failed")
         self.handle = h
-        self.work_bytes = {}  # zs_rmsnorm_bwd_work by the bytes of the rows and the weight
+        self.work_bytes = {}  # zs_rmsnorm_bwd_work by (rows, cols)
 
     def check(self, rc: int):
         if rc != ZS_OK:
@@ -825,8 +831,9 @@ def make_norm_shape(rows: int, cols: int, dt, eps: float, bits: int = 16, group:
                     x_stride: int = 0, residual_stride: int = 0, sum_stride: int = 0,
                     out_stride: int = 0, dy_stride: int = 0, dx_stride: int = 0) -> zs_norm_shape:
     """Strides in elements from one row to the next; 0: the rows are contiguous."""
-    return zs_norm_shape(rows, cols, _dtype(dt), bits, group, eps, x_stride, residual_stride,
-                         sum_stride, out_stride, dy_stride, dx_stride)
+    return zs_norm_shape.from_buffer_copy(_NORM_SHAPE.pack(
+        rows, cols, _dtype(dt), bits, group, eps, x_stride, residual_stride, sum_stride,
+        out_stride, dy_stride, dx_stride))
 
 
 def _norm_holds(shape):
@@ -875,6 +882,7 @@ def zs_rmsnorm_bwd_work(ctx: Ctx, shape: zs_norm_shape) -> int:
     """Bytes of workspace zs_rmsnorm_bwd needs for this shape."""
     n = ctypes.c_int64()
     ctx.check(lib.zs_rmsnorm_bwd_work(ctx.handle, ctypes.byref(shape), ctypes.byref(n)))
+    ctx.work_bytes[shape.rows, shape.cols] = n.value
     return n.value
 
 
@@ -892,9 +900,9 @@ def zs_rmsnorm_bwd(ctx: Ctx, shape: zs_norm_shape, dy, h, rstd, weight, dsum, dx
              _rows(h, "h", half, rows, cols, shape.x_stride))
         b = (_rows(dsum, "dsum", half, rows, cols, shape.residual_stride),
              _rows(dx, "dx", half, rows, cols, shape.dx_stride))
-    need = ctx.work_bytes.get((n, n_weight))  # (rows and columns, in bytes)
+    need = ctx.work_bytes.get((shape.rows, shape.cols))
     if need is None and hasattr(work, "nbytes"):
-        need = ctx.work_bytes[n, n_weight] = zs_rmsnorm_bwd_work(ctx, shape)
+        need = zs_rmsnorm_bwd_work(ctx, shape)
     rc = lib.zs_rmsnorm_bwd(ctx.handle, ctypes.byref(shape), *a,
                             _fitting(rstd, "rstd", fp32, n_rows),
                             _fitting(weight, "weight", half, n_weight), *b,
